@@ -812,6 +812,7 @@ __global__ void __launch_bounds__(32 * kW + 64, kW == 4 ? 5 : kW == 16 ? 1 : kH 
             const float weight = p.weight ? p.weight[row] : 1.f;
             const float mass = teacher_mass(p, ex, s.q[slot]);
             const RowTeacher teacher = row_teacher(p, mass, weight);
+            __syncwarp();   // every lane's q, which lane 0's arrival on `known` publishes
             if (!wait(s.exchanged, n, kSlots, true)) break;
             const RowTotals t = row_totals(p, ex, s.part[slot], C * kW, teacher);
             if (lane == 0) {
