@@ -407,8 +407,11 @@ ws_status ws_distill_validate(const ws_distill_desc* desc);
  *           them.  A q' below 2^-20 is rounding of the log probabilities and
  *           counts as 0.  (The 1 is sum q + q', which rounding may leave a
  *           little off 1.)
- * Where the student's probability is 0 and the teacher's is not, L is +inf
- * and the gradient stays as the formulas give it (p_j = 0).  A row in which
+ * Where the student masks what the teacher gives mass (an entry, or with
+ * WS_DISTILL_TAIL everything off the entries), L is +inf and the gradient stays
+ * as the formulas give it (p_j = 0).  A student's probability that is merely too
+ * small for float32 is no such 0: L and p_j/p' stay what they are, however far
+ * the student is from its teacher.  A row in which
  * the student has nothing left, or the teacher has no entry, has loss 0 and
  * gradient 0 (without entries in TAIL mode all mass is tail on both sides).
  * The gradient is computed in the same launch as the loss.  Rows are kept in

@@ -88,7 +88,7 @@ struct RowExchange {
 
 struct __align__(16) TiledShared {
     RowExchange row;
-    float m, scale, on, wt;         // of the row's totals
+    float m, m_off, scale, on, wt;  // of the row's totals
     SoftSums part[kWarps];          // the warps' sums
     float2 block[8];                // every block's maximum and sum
     float q[kMaxK];                 // the teacher's probabilities
@@ -150,11 +150,19 @@ __device__ __forceinline__ RowTeacher row_teacher(const DistillParams& p, float 
 }
 
 // What a row's loss and gradient are made of, in every lane of a warp.
+//
+// The sums off the teacher's columns stay relative to the largest logit there:
+// a student that is sure of the teacher's columns has a mass off them that no
+// float32 holds (2^-126 is a gap of 87 temperatures), but the tail's share
+// of the gradient is the teacher's remaining mass spread by what each entry is
+// of that mass, and the loss takes its logarithm.
 struct RowTotals {
     float m;         // the largest logit
-    float off;       // the sums relative to it: off the teacher's columns, ...
-    float total;     // ... over all
-    float scale;     // an entry off the teacher's columns: scale 2^((x - m) c)
+    float m_off;     // ... off the teacher's columns
+    float off;       // the sum off them, relative to m_off
+    float per_off;   // 2^((m_off - m) c): off is off * per_off relative to m
+    float total;     // the sum over all, relative to m
+    float scale;     // an entry off the teacher's columns: scale 2^((x - m_off) c)
     float on;        // an entry on them: on 2^((x - m) c) - wt q
     float wt;
 };
@@ -170,14 +178,15 @@ __device__ __forceinline__ RowTotals row_totals(const DistillParams& p, const Ro
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lane + 32 * i < n ? part[lane + 32 * i] : make_float2(-INFINITY, 0.f);
     const float x = lane < p.k ? r.x[lane] : -INFINITY;
-    float m = fmaxf(fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), x);
-    for (int i = lane + 128; i < n; i += 32) m = fmaxf(m, part[i].x);
-    for (int k = lane + 32; k < p.k; k += 32) m = fmaxf(m, r.x[k]);
-    t.m = order_value(__reduce_max_sync(0xffffffffu, order_bits(m)));
+    float m_off = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x)), m_on = x;
+    for (int i = lane + 128; i < n; i += 32) m_off = fmaxf(m_off, part[i].x);
+    for (int k = lane + 32; k < p.k; k += 32) m_on = fmaxf(m_on, r.x[k]);
+    t.m_off = order_value(__reduce_max_sync(0xffffffffu, order_bits(m_off)));
+    t.m = fmaxf(t.m_off, order_value(__reduce_max_sync(0xffffffffu, order_bits(m_on))));
     float off = 0.f, on = exp2_fast(below(x, t.m) * p.c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) off += v[i].y * exp2_fast(below(v[i].x, t.m) * p.c);
-    for (int i = lane + 128; i < n; i += 32) off += part[i].y * exp2_fast(below(part[i].x, t.m) * p.c);
+    for (int i = 0; i < 4; ++i) off += v[i].y * exp2_fast(below(v[i].x, t.m_off) * p.c);
+    for (int i = lane + 128; i < n; i += 32) off += part[i].y * exp2_fast(below(part[i].x, t.m_off) * p.c);
     for (int k = lane + 32; k < p.k; k += 32) on += exp2_fast(below(r.x[k], t.m) * p.c);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -185,12 +194,13 @@ __device__ __forceinline__ RowTotals row_totals(const DistillParams& p, const Ro
         on += __shfl_xor_sync(0xffffffffu, on, o);
     }
     t.off = off;
-    t.total = off + on;
+    t.per_off = exp2_fast(below(t.m_off, t.m) * p.c);
+    t.total = off * t.per_off + on;
     t.wt = teacher.wt;
-    const float per_e = __fdividef(t.wt, t.total);   // 2 ulp
-    t.on = teacher.whole * per_e;
-    t.scale = t.on;
-    if (teacher.rest > 0.f && off > 0.f) t.scale -= teacher.rest * __fdividef(t.total, off) * per_e;
+    t.on = teacher.whole * __fdividef(t.wt, t.total);   // 2 ulp
+    t.scale = t.on * t.per_off;
+    // off is 1 at least where anything is left off the teacher's columns
+    if (teacher.rest > 0.f && t.m_off > -INFINITY) t.scale -= t.wt * __fdividef(teacher.rest, off);
     if (t.m == -INFINITY) t.scale = t.on = t.wt = 0.f;   // the student has nothing left
     if (t.m == INFINITY) t.scale = t.on = NAN;
     return t;
@@ -223,10 +233,13 @@ __device__ __forceinline__ float row_loss(const DistillParams& p, const RowExcha
     }
     float loss = term;
     if (teacher.rest > 0.f) {
-        if (t.off > 0.f) {
-            // ln(rest / p_off) by their difference while that is the exact one
-            const float p_off = t.off * per_total, rel = more / p_off;
-            loss += teacher.rest * (rel > -0.5f ? log1pf(rel) : logf(teacher.rest) - logf(p_off));
+        if (t.m_off > -INFINITY) {
+            // ln(rest / p_off) by their difference while that is the exact
+            // one, else by their logarithms (p_off itself may be below 2^-126)
+            const float rel = more / (t.off * t.per_off * per_total);
+            loss += teacher.rest * (rel > -0.5f && rel < 1.f
+                                        ? log1pf(rel)
+                                        : logf(teacher.rest) - ((t.m_off - t.m) * p.inv_t + (logf(t.off) - ln_s)));
         } else {
             loss = INFINITY;
         }
@@ -500,7 +513,7 @@ __global__ void __launch_bounds__(128, 4) distill_short_kernel(const __grid_cons
     const float loss = row_loss(p, s.row, s.q, t, teacher, weight);
     if (lane == 0) p.loss[row] = loss;
     if (!gr) return;
-    store_run<E, kH>(p, gr, rb.lead, 0, nvec, lane, 32, e, t.scale * exp2_fast(below(m, t.m) * p.c));
+    store_run<E, kH>(p, gr, rb.lead, 0, nvec, lane, 32, e, t.scale * exp2_fast(below(m, t.m_off) * p.c));
     __syncwarp();   // the zeros at the teacher's columns are written
     for (int k = lane; k < p.k; k += 32) {
         if (k >= 32 || p.k > 32) load_entry(k);
@@ -523,7 +536,8 @@ template <int kW, int kH>
 struct __align__(16) Shared {
     RowExchange row[kSlots];             // the live rows in turn
     float q[kSlots][kMaxK];              // the teacher's probabilities
-    float4 totals[kSlots];               // m, scale, on, wt of the row's totals
+    float4 totals[kSlots];               // m_off, scale, m, on of the row's totals
+    float wt[kSlots];                    // ... and wt
     float2 part[kSlots][kMaxCluster * kW];   // every block's every streaming warp's maximum and sum
     int own[kSlots][kMaxK];              // the teacher's columns in this block's run: entry of the run | k << 20
     int owned[kSlots];                   // how many
@@ -670,13 +684,14 @@ __global__ void __launch_bounds__(32 * kW + 64, kW == 4 ? 5 : kW == 16 ? 1 : kH 
                 const int v0 = s.place[slot].v0;
                 const float4 of = s.totals[slot];
                 RowTotals t;
-                t.m = of.x;
+                t.m_off = of.x;
                 t.scale = of.y;
-                t.on = of.z;
-                t.wt = of.w;
+                t.m = of.z;
+                t.on = of.w;
+                t.wt = s.wt[slot];
                 S* gr = grad_of(s.place[slot].row);
                 const int lead = s.place[slot].lead;
-                store_run<E, kH>(p, gr, lead, v0, nv, tid, kStream, e, t.scale * exp2_fast(below(m, t.m) * p.c));
+                store_run<E, kH>(p, gr, lead, v0, nv, tid, kStream, e, t.scale * exp2_fast(below(m, t.m_off) * p.c));
                 // the teacher's columns among this warp's vectors, after the
                 // warp's zeros there
                 __syncwarp();
@@ -816,7 +831,8 @@ __global__ void __launch_bounds__(32 * kW + 64, kW == 4 ? 5 : kW == 16 ? 1 : kH 
             if (!wait(s.exchanged, n, kSlots, true)) break;
             const RowTotals t = row_totals(p, ex, s.part[slot], C * kW, teacher);
             if (lane == 0) {
-                s.totals[slot] = make_float4(t.m, t.scale, t.on, t.wt);
+                s.totals[slot] = make_float4(t.m_off, t.scale, t.m, t.on);
+                s.wt[slot] = t.wt;
                 mbar_arrive(&s.known[slot]);
             }
             __syncwarp();
@@ -953,6 +969,7 @@ __global__ void __launch_bounds__(kThreads) distill_tiled_kernel(const __grid_co
         if (rank == 0 && lane == 0) p.loss[row] = loss;
         if (lane == 0) {
             s.m = t.m;
+            s.m_off = t.m_off;
             s.scale = t.scale;
             s.on = t.on;
             s.wt = t.wt;
@@ -964,7 +981,7 @@ __global__ void __launch_bounds__(kThreads) distill_tiled_kernel(const __grid_co
             const int n = min(p.tile, v1 - t0);
             fetch(t0, n);
             patch(t0, n, false);
-            write_gradient<E>(p, gr, rb, buf, t0, n, s.m, dead ? NAN : s.scale, tid, kThreads);
+            write_gradient<E>(p, gr, rb, buf, t0, n, s.m_off, dead ? NAN : s.scale, tid, kThreads);
         }
         __syncthreads();   // the gradient at the teacher's columns is written
         if (my_v >= v0 && my_v < v1) {
