@@ -124,17 +124,37 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _keep(stream, device: int, *tensors) -> int:
-    """The raw stream; on a stream other than the current one the tensors' memory is held until its work is done."""
+def _other_stream(stream, device: int):
+    """The stream of a call's `stream` argument (a Stream or a raw one), None where it is the device's current one."""
     if stream is None:
-        return _current_stream(device)
+        return None
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    if stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    return stream.cuda_stream
+    return None if stream.cuda_stream == _current_stream(device) else stream
+
+
+def _results(other, make):
+    """make()'s tensors.  For a call on another stream they come from that stream's memory: a block of the current
+    stream's may still be read by work queued there under its last owner.  They are held for both streams."""
+    if other is None:
+        return make()
+    with torch.cuda.stream(other):
+        out = make()
+    current = torch.cuda.current_stream()
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(current)
+    return out
+
+
+def _keep(other, device: int, *tensors) -> int:
+    """The raw stream; on a stream other than the current one the tensors' memory is held until its work is done."""
+    if other is None:
+        return _current_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
+    return other.cuda_stream
 
 
 def _new_logprobs(rows: int, k: int, with_tokens: bool, device) -> Logprobs:
@@ -151,8 +171,10 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
     padded.  tokens: int32 or int64 [rows], negative where a row has none.  out: an earlier result of the same
     call to write into."""
     rows, cols, stride, dtype = _matrix(logits, "logits")
+    device = logits.get_device()
+    other = _other_stream(stream, device)
     if out is None:
-        out = _new_logprobs(rows, k, tokens is not None, logits.device)
+        out = _results(other, lambda: _new_logprobs(rows, k, tokens is not None, logits.device))
     per_row = (rows,)
     tok = _operand(tokens, "tokens", per_row, _INDEX_TYPES)
     desc = B.ws_logprobs_desc(rows, cols, stride, dtype, _INDEX_TYPES[tokens.dtype] if tokens is not None else 0, k,
@@ -163,7 +185,7 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
                           _operand(out.stats, "out.stats", (rows, 2), _F32),
                           _operand(out.top_logprob, "out.top_logprob", (rows, k), _F32),
                           _operand(out.top_idx, "out.top_idx", (rows, k), _I32),
-                          _keep(stream, logits.get_device(), logits, tokens, *out)))
+                          _keep(other, device, logits, tokens, *out)))
     return out
 
 
@@ -175,8 +197,10 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats: 
     (either may be None); stats and entropy as logprobs() gave them.  out: a tensor of the logits' shape and type
     whose rows may be padded, the logits themselves included."""
     rows, cols, stride, dtype = _matrix(logits, "logits")
+    device = logits.get_device()
+    other = _other_stream(stream, device)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _results(other, lambda: torch.empty(logits.shape, dtype=logits.dtype, device=logits.device))
     out_rows, out_cols, out_stride, out_dtype = _matrix(out, "out")
     if (out_rows, out_cols, out_dtype) != (rows, cols, dtype):
         raise ValueError("out has another shape or type than the logits")
@@ -188,7 +212,7 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats: 
                                    _operand(entropy, "entropy", per_row, _F32),
                                    _operand(grad_logprob, "grad_logprob", per_row, _F32),
                                    _operand(grad_entropy, "grad_entropy", per_row, _F32), out.data_ptr(), out_stride,
-                                   _keep(stream, logits.get_device(), logits, tokens, stats, entropy, grad_logprob, grad_entropy, out)))
+                                   _keep(other, device, logits, tokens, stats, entropy, grad_logprob, grad_entropy, out)))
     return out
 
 
@@ -202,9 +226,12 @@ def distill(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logprob: to
     if teacher_idx.dim() != logits.dim():
         raise ValueError("teacher_idx must have as many dimensions as the logits")
     k = teacher_idx.shape[-1]
+    device = logits.get_device()
+    other = _other_stream(stream, device)
     if out is None:
-        out = Distill(torch.empty(rows, dtype=torch.float32, device=logits.device),
-                      torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if grad else None)
+        out = _results(other, lambda: Distill(
+            torch.empty(rows, dtype=torch.float32, device=logits.device),
+            torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if grad else None))
     gptr, gstride = None, cols
     if out.grad is not None:
         g_rows, g_cols, gstride, g_dtype = _matrix(out.grad, "out.grad")
@@ -217,7 +244,7 @@ def distill(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logprob: to
                              B.WS_DISTILL_TAIL if tail else B.WS_DISTILL_RENORM, temperature)
     B.check(B.ws_distill(desc, logits.data_ptr(), ids, _operand(teacher_logprob, "teacher_logprob", entries, _F32),
                          _operand(weight, "weight", (rows,), _F32), _operand(out.loss, "out.loss", (rows,), _F32), gptr,
-                         _keep(stream, logits.get_device(), logits, teacher_idx, teacher_logprob, weight, *out)))
+                         _keep(other, device, logits, teacher_idx, teacher_logprob, weight, *out)))
     return out
 
 
