@@ -12,10 +12,49 @@ import torch
 from . import binding as B
 
 
-def _stream(stream) -> int:
+# the current stream of a device as an integer: torch's own accessor where it has one, as it costs a thirtieth of
+# making a Stream object
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _other_stream(stream, device: int):
+    """The stream of a call's `stream` argument (a Stream or a raw one), None where it is the device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return None
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return None if stream.cuda_stream == _current_stream(device) else stream
+
+
+def _results(other, make):
+    """make()'s tensors.  For a call on another stream they come from that stream's memory: a block of the current
+    stream's may still be read by work queued there under its last owner.  They are held for both streams."""
+    if other is None:
+        return make()
+    with torch.cuda.stream(other):
+        out = make()
+    current = torch.cuda.current_stream()
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(current)
+    return out
+
+
+def _keep(other, device: int, *tensors) -> int:
+    """The raw stream; on a stream other than the current one the tensors' memory is held until its work is done."""
+    if other is None:
+        return _current_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
+    return other.cuda_stream
+
+
+def _index(device) -> int:
+    """The number of a CUDA device given as torch takes it ("cuda": the current one)."""
+    index = torch.device(device).index
+    return torch.cuda.current_device() if index is None else index
 
 
 def preprocess(frames: torch.Tensor, desc: B.ws_preprocess_desc, batch: int | None = None,
@@ -25,12 +64,23 @@ def preprocess(frames: torch.Tensor, desc: B.ws_preprocess_desc, batch: int | No
         raise TypeError("frames must be a uint8 CUDA tensor")
     if batch is None:
         batch = frames.shape[0]
+    device = frames.get_device()
+    other = _other_stream(stream, device)
     if out is None:
         dtype = {B.WS_DTYPE_F32: torch.float32, B.WS_DTYPE_F16: torch.float16,
                  B.WS_DTYPE_BF16: torch.bfloat16}[desc.dst_type]
-        out = torch.empty((batch, 3, desc.dst_h, desc.dst_w), dtype=dtype, device=frames.device)
-    B.check(B.ws_preprocess(desc, frames.data_ptr(), batch, out.data_ptr(), _stream(stream)))
+        out = _results(other, lambda: torch.empty((batch, 3, desc.dst_h, desc.dst_w), dtype=dtype, device=frames.device))
+    B.check(B.ws_preprocess(desc, frames.data_ptr(), batch, out.data_ptr(), _keep(other, device, frames, out)))
     return out
+
+
+def _workspace(n: int, device, stream):
+    """n bytes at a 256-byte boundary, and the raw stream of a call's `stream` argument, from whose memory they come."""
+    index = _index(device)
+    other = _other_stream(stream, index)
+    ws = _results(other, lambda: torch.empty(n + 256, dtype=torch.uint8, device=device))
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n], _keep(other, index)
 
 
 def topk_workspace(rows: int, cols: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
@@ -39,10 +89,8 @@ def topk_workspace(rows: int, cols: int, k: int, device="cuda", stream=None) -> 
     B.check(st)
     if n == 0:
         return None
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-ws.data_ptr()) % 256
-    ws = ws[off:off + n]
-    B.check(B.ws_topk_workspace_init(ws.data_ptr(), n, _stream(stream)))
+    ws, raw = _workspace(n, device, stream)
+    B.check(B.ws_topk_workspace_init(ws.data_ptr(), n, raw))
     return ws
 
 
@@ -52,15 +100,17 @@ def topk(x: torch.Tensor, k: int, out_val: torch.Tensor | None = None, out_idx: 
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise TypeError("x must be a contiguous float32 CUDA tensor")
     rows, cols = (1, x.shape[0]) if x.dim() == 1 else x.shape
+    device = x.get_device()
+    other = _other_stream(stream, device)
     if out_val is None:
-        out_val = torch.empty((rows, k), dtype=torch.float32, device=x.device)
+        out_val = _results(other, lambda: torch.empty((rows, k), dtype=torch.float32, device=x.device))
     if out_idx is None:
-        out_idx = torch.empty((rows, k), dtype=torch.int32, device=x.device)
+        out_idx = _results(other, lambda: torch.empty((rows, k), dtype=torch.int32, device=x.device))
     if workspace is None:
         workspace = topk_workspace(rows, cols, k, x.device, stream)
     wptr, wbytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     B.check(B.ws_topk(x.data_ptr(), rows, cols, k, out_val.data_ptr(), out_idx.data_ptr(), wptr, wbytes,
-                      _stream(stream)))
+                      _keep(other, device, x, out_val, out_idx, workspace)))
     return out_val, out_idx
 
 
@@ -118,45 +168,6 @@ def _operand(t: torch.Tensor | None, name: str, shape: tuple, dtypes):
 
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
-# the current stream of a device as an integer: torch's own accessor where it has one, as it costs a thirtieth of
-# making a Stream object
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
-
-
-def _other_stream(stream, device: int):
-    """The stream of a call's `stream` argument (a Stream or a raw one), None where it is the device's current one."""
-    if stream is None:
-        return None
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return None if stream.cuda_stream == _current_stream(device) else stream
-
-
-def _results(other, make):
-    """make()'s tensors.  For a call on another stream they come from that stream's memory: a block of the current
-    stream's may still be read by work queued there under its last owner.  They are held for both streams."""
-    if other is None:
-        return make()
-    with torch.cuda.stream(other):
-        out = make()
-    current = torch.cuda.current_stream()
-    for t in out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(current)
-    return out
-
-
-def _keep(other, device: int, *tensors) -> int:
-    """The raw stream; on a stream other than the current one the tensors' memory is held until its work is done."""
-    if other is None:
-        return _current_stream(device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(other)
-    return other.cuda_stream
-
-
 def _new_logprobs(rows: int, k: int, with_tokens: bool, device) -> Logprobs:
     """Results in one allocation (each tensor contiguous)."""
     logprob, entropy, lse, stats, top = torch.empty(rows * (5 + k), dtype=torch.float32, device=device).split(
@@ -252,10 +263,8 @@ def detect_workspace(desc: B.ws_detect_desc, batch: int, device="cuda", stream=N
     """A zeroed, 256-byte aligned workspace for ws_detect of this geometry and batch."""
     st, n = B.ws_detect_workspace_bytes(desc, batch)
     B.check(st)
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-ws.data_ptr()) % 256
-    ws = ws[off:off + n]
-    B.check(B.ws_detect_workspace_init(ws.data_ptr(), n, _stream(stream)))
+    ws, raw = _workspace(n, device, stream)
+    B.check(B.ws_detect_workspace_init(ws.data_ptr(), n, raw))
     return ws
 
 
@@ -271,12 +280,14 @@ def detect(head: torch.Tensor, desc: B.ws_detect_desc, workspace: torch.Tensor |
     batch = head.shape[0]
     if workspace is None:
         workspace = detect_workspace(desc, batch, head.device, stream)
+    device = head.get_device()
+    other = _other_stream(stream, device)
     if out is None:
-        out = torch.empty((batch, desc.max_det, 8), dtype=torch.int32, device=head.device)
+        out = _results(other, lambda: torch.empty((batch, desc.max_det, 8), dtype=torch.int32, device=head.device))
     if out_count is None:
-        out_count = torch.empty(batch, dtype=torch.int32, device=head.device)
+        out_count = _results(other, lambda: torch.empty(batch, dtype=torch.int32, device=head.device))
     B.check(B.ws_detect(desc, head.data_ptr(), batch, out.data_ptr(), out_count.data_ptr(), workspace.data_ptr(),
-                        workspace.numel(), _stream(stream)))
+                        workspace.numel(), _keep(other, device, head, out, out_count, workspace)))
     return out, out_count
 
 

@@ -72,3 +72,23 @@ def test_a_result_freed_early_is_held_for_its_readers(pp):
     s.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+def test_topk(pp):
+    rows, cols, k = 64, 200000, 32
+    x = torch.randn((rows, cols), device="cuda")
+    val, idx = pp.topk(x, k)
+    torch.cuda.synchronize()
+    assert pp.topk_workspace(rows, cols, k) is not None
+    for elems in (rows * k, rows * cols // 16):
+        v, i = check(elems, torch.float32, lambda s: pp.topk(x, k, stream=s))
+        assert torch.equal(v, val) and torch.equal(i, idx)
+
+
+def test_preprocess(pp):
+    B = pp.binding
+    desc = B.preprocess_desc(640, 480, 224, 224)
+    frames = torch.randint(0, 256, (8, 480, 640, 3), dtype=torch.uint8, device="cuda")
+    want = pp.preprocess(frames, desc)
+    torch.cuda.synchronize()
+    assert torch.equal(check(8 * 3 * 224 * 224, torch.float32, lambda s: pp.preprocess(frames, desc, stream=s)), want)
