@@ -18,22 +18,34 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(device: int, name: str) -> ValueError:
+    """A call runs on its main operand's device, which has to be the current one, as the library launches there."""
+    return ValueError(f"{name} is on cuda:{device}, the current device is cuda:{_current_device()}")
+
+
 def _other_stream(stream, device: int):
     """The stream of a call's `stream` argument (a Stream or a raw one), None where it is the device's current one."""
-    if stream is None:
-        return None
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the call runs on cuda:{device}")
     return None if stream.cuda_stream == _current_stream(device) else stream
 
 
-def _results(other, make):
-    """make()'s tensors.  For a call on another stream they come from that stream's memory: a block of the current
+def _empty(shape, dtype, device) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _results(other, make, *args):
+    """make(*args): a call's results.  For a call on another stream they come from that stream's memory: a block of the current
     stream's may still be read by work queued there under its last owner.  They are held for both streams."""
     if other is None:
-        return make()
+        return make(*args)
     with torch.cuda.stream(other):
-        out = make()
+        out = make(*args)
     current = torch.cuda.current_stream()
     for t in out if isinstance(out, tuple) else (out,):
         if t is not None:
@@ -41,20 +53,12 @@ def _results(other, make):
     return out
 
 
-def _keep(other, device: int, *tensors) -> int:
-    """The raw stream; on a stream other than the current one the tensors' memory is held until its work is done."""
-    if other is None:
-        return _current_stream(device)
+def _held(other, *tensors) -> int:
+    """The raw handle of a stream other than the current one, for whose work the tensors' memory is held."""
     for t in tensors:
         if t is not None:
             t.record_stream(other)
     return other.cuda_stream
-
-
-def _index(device) -> int:
-    """The number of a CUDA device given as torch takes it ("cuda": the current one)."""
-    index = torch.device(device).index
-    return torch.cuda.current_device() if index is None else index
 
 
 def preprocess(frames: torch.Tensor, desc: B.ws_preprocess_desc, batch: int | None = None,
@@ -65,22 +69,28 @@ def preprocess(frames: torch.Tensor, desc: B.ws_preprocess_desc, batch: int | No
     if batch is None:
         batch = frames.shape[0]
     device = frames.get_device()
-    other = _other_stream(stream, device)
+    if device != _current_device():
+        raise _elsewhere(device, "frames")
+    other = None if stream is None else _other_stream(stream, device)
     if out is None:
         dtype = {B.WS_DTYPE_F32: torch.float32, B.WS_DTYPE_F16: torch.float16,
                  B.WS_DTYPE_BF16: torch.bfloat16}[desc.dst_type]
-        out = _results(other, lambda: torch.empty((batch, 3, desc.dst_h, desc.dst_w), dtype=dtype, device=frames.device))
-    B.check(B.ws_preprocess(desc, frames.data_ptr(), batch, out.data_ptr(), _keep(other, device, frames, out)))
+        out = _results(other, _empty, (batch, 3, desc.dst_h, desc.dst_w), dtype, frames.device)
+    B.check(B.ws_preprocess(desc, frames.data_ptr(), batch, out.data_ptr(),
+                            _current_stream(device) if other is None else _held(other, frames, out)))
     return out
 
 
 def _workspace(n: int, device, stream):
     """n bytes at a 256-byte boundary, and the raw stream of a call's `stream` argument, from whose memory they come."""
-    index = _index(device)
-    other = _other_stream(stream, index)
-    ws = _results(other, lambda: torch.empty(n + 256, dtype=torch.uint8, device=device))
+    index = torch.device(device).index
+    if index not in (None, _current_device()):
+        raise _elsewhere(index, "a workspace")
+    index = _current_device()
+    other = None if stream is None else _other_stream(stream, index)
+    ws = _results(other, _empty, (n + 256,), torch.uint8, device)
     off = (-ws.data_ptr()) % 256
-    return ws[off:off + n], _keep(other, index)
+    return ws[off:off + n], _current_stream(index) if other is None else other.cuda_stream
 
 
 def topk_workspace(rows: int, cols: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
@@ -101,16 +111,18 @@ def topk(x: torch.Tensor, k: int, out_val: torch.Tensor | None = None, out_idx: 
         raise TypeError("x must be a contiguous float32 CUDA tensor")
     rows, cols = (1, x.shape[0]) if x.dim() == 1 else x.shape
     device = x.get_device()
-    other = _other_stream(stream, device)
+    if device != _current_device():
+        raise _elsewhere(device, "x")
+    other = None if stream is None else _other_stream(stream, device)
     if out_val is None:
-        out_val = _results(other, lambda: torch.empty((rows, k), dtype=torch.float32, device=x.device))
+        out_val = _results(other, _empty, (rows, k), torch.float32, x.device)
     if out_idx is None:
-        out_idx = _results(other, lambda: torch.empty((rows, k), dtype=torch.int32, device=x.device))
+        out_idx = _results(other, _empty, (rows, k), torch.int32, x.device)
     if workspace is None:
         workspace = topk_workspace(rows, cols, k, x.device, stream)
     wptr, wbytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     B.check(B.ws_topk(x.data_ptr(), rows, cols, k, out_val.data_ptr(), out_idx.data_ptr(), wptr, wbytes,
-                      _keep(other, device, x, out_val, out_idx, workspace)))
+                      _current_stream(device) if other is None else _held(other, x, out_val, out_idx, workspace)))
     return out_val, out_idx
 
 
@@ -136,9 +148,9 @@ class Distill(NamedTuple):
 
 
 def _matrix(x: torch.Tensor, name: str):
-    """(rows, cols, row stride, type) of a CUDA tensor [rows, cols] whose rows are contiguous, or [cols]."""
-    dtype = _DTYPES.get(x.dtype)
-    if dtype is None or not x.is_cuda:
+    """(rows, cols, row stride, type, device) of a CUDA tensor [rows, cols] whose rows are contiguous, or [cols]."""
+    dtype, device = _DTYPES.get(x.dtype), x.get_device()
+    if dtype is None or device < 0:
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 CUDA tensor")
     shape = x.shape
     if len(shape) == 2:
@@ -153,21 +165,25 @@ def _matrix(x: torch.Tensor, name: str):
         raise TypeError(f"{name} must be [rows, cols] or [cols]")
     if step != 1 and cols > 1:
         raise TypeError(f"{name}'s rows must be contiguous")
-    return rows, cols, stride, dtype
+    return rows, cols, stride, dtype, device
 
 
-def _operand(t: torch.Tensor | None, name: str, shape: tuple, dtypes):
-    """The address of a contiguous CUDA tensor of this shape and one of these types (None for None)."""
+def _operand(t: torch.Tensor | None, name: str, shape: tuple, dtypes, device: int):
+    """The address of a contiguous tensor of this shape and one of these types on this device (None for None)."""
     if t is None:
         return None
+    if t.get_device() == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, {shape} expected")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on another device than the call's cuda:{device}")
 
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
+
+
 def _new_logprobs(rows: int, k: int, with_tokens: bool, device) -> Logprobs:
     """Results in one allocation (each tensor contiguous)."""
     logprob, entropy, lse, stats, top = torch.empty(rows * (5 + k), dtype=torch.float32, device=device).split(
@@ -176,27 +192,35 @@ def _new_logprobs(rows: int, k: int, with_tokens: bool, device) -> Logprobs:
                     torch.empty((rows, k), dtype=torch.int32, device=device) if k else None)
 
 
+def _new_distill(rows: int, logits: torch.Tensor, grad: bool) -> Distill:
+    return Distill(_empty((rows,), torch.float32, logits.device),
+                   _empty(logits.shape, logits.dtype, logits.device) if grad else None)
+
+
 def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, temperature: float = 1.0,
              out: Logprobs | None = None, stream=None) -> Logprobs:
     """ws_logprobs on a CUDA tensor [rows, cols] (or [cols]) of float32, float16 or bfloat16, whose rows may be
     padded.  tokens: int32 or int64 [rows], negative where a row has none.  out: an earlier result of the same
     call to write into."""
-    rows, cols, stride, dtype = _matrix(logits, "logits")
-    device = logits.get_device()
-    other = _other_stream(stream, device)
+    rows, cols, stride, dtype, device = _matrix(logits, "logits")
+    if device != _current_device():
+        raise _elsewhere(device, "logits")
+    other = None if stream is None else _other_stream(stream, device)
     if out is None:
-        out = _results(other, lambda: _new_logprobs(rows, k, tokens is not None, logits.device))
+        out = _results(other, _new_logprobs, rows, k, tokens is not None, logits.device)
     per_row = (rows,)
-    tok = _operand(tokens, "tokens", per_row, _INDEX_TYPES)
+    tok = _operand(tokens, "tokens", per_row, _INDEX_TYPES, device)
     desc = B.ws_logprobs_desc(rows, cols, stride, dtype, _INDEX_TYPES[tokens.dtype] if tokens is not None else 0, k,
                               temperature)
-    B.check(B.ws_logprobs(desc, logits.data_ptr(), tok, _operand(out.logprob, "out.logprob", per_row, _F32),
-                          _operand(out.entropy, "out.entropy", per_row, _F32),
-                          _operand(out.lse, "out.lse", per_row, _F32),
-                          _operand(out.stats, "out.stats", (rows, 2), _F32),
-                          _operand(out.top_logprob, "out.top_logprob", (rows, k), _F32),
-                          _operand(out.top_idx, "out.top_idx", (rows, k), _I32),
-                          _keep(other, device, logits, tokens, *out)))
+    status = B.ws_logprobs(desc, logits.data_ptr(), tok, _operand(out.logprob, "out.logprob", per_row, _F32, device),
+                           _operand(out.entropy, "out.entropy", per_row, _F32, device),
+                           _operand(out.lse, "out.lse", per_row, _F32, device),
+                           _operand(out.stats, "out.stats", (rows, 2), _F32, device),
+                           _operand(out.top_logprob, "out.top_logprob", (rows, k), _F32, device),
+                           _operand(out.top_idx, "out.top_idx", (rows, k), _I32, device),
+                           _current_stream(device) if other is None else _held(other, logits, tokens, *out))
+    if status:
+        B.check(status)
     return out
 
 
@@ -207,23 +231,29 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats: 
     """ws_logprobs_backward: the gradient of the logits from those of logprobs()' log probabilities and entropies
     (either may be None); stats and entropy as logprobs() gave them.  out: a tensor of the logits' shape and type
     whose rows may be padded, the logits themselves included."""
-    rows, cols, stride, dtype = _matrix(logits, "logits")
-    device = logits.get_device()
-    other = _other_stream(stream, device)
+    rows, cols, stride, dtype, device = _matrix(logits, "logits")
+    if device != _current_device():
+        raise _elsewhere(device, "logits")
+    other = None if stream is None else _other_stream(stream, device)
     if out is None:
-        out = _results(other, lambda: torch.empty(logits.shape, dtype=logits.dtype, device=logits.device))
-    out_rows, out_cols, out_stride, out_dtype = _matrix(out, "out")
+        out = _results(other, _empty, logits.shape, logits.dtype, logits.device)
+    out_rows, out_cols, out_stride, out_dtype, where = _matrix(out, "out")
+    if where != device:
+        raise ValueError(f"out is on another device than the call's cuda:{device}")
     if (out_rows, out_cols, out_dtype) != (rows, cols, dtype):
         raise ValueError("out has another shape or type than the logits")
     per_row = (rows,)
     desc = B.ws_logprobs_desc(rows, cols, stride, dtype, _INDEX_TYPES.get(tokens.dtype, 0) if tokens is not None else 0,
                               0, temperature)
-    B.check(B.ws_logprobs_backward(desc, logits.data_ptr(), _operand(tokens, "tokens", per_row, _INDEX_TYPES),
-                                   _operand(stats, "stats", (rows, 2), _F32),
-                                   _operand(entropy, "entropy", per_row, _F32),
-                                   _operand(grad_logprob, "grad_logprob", per_row, _F32),
-                                   _operand(grad_entropy, "grad_entropy", per_row, _F32), out.data_ptr(), out_stride,
-                                   _keep(other, device, logits, tokens, stats, entropy, grad_logprob, grad_entropy, out)))
+    status = B.ws_logprobs_backward(desc, logits.data_ptr(), _operand(tokens, "tokens", per_row, _INDEX_TYPES, device),
+                                    _operand(stats, "stats", (rows, 2), _F32, device),
+                                    _operand(entropy, "entropy", per_row, _F32, device),
+                                    _operand(grad_logprob, "grad_logprob", per_row, _F32, device),
+                                    _operand(grad_entropy, "grad_entropy", per_row, _F32, device), out.data_ptr(),
+                                    out_stride, _current_stream(device) if other is None else _held(
+                                        other, logits, tokens, stats, entropy, grad_logprob, grad_entropy, out))
+    if status:
+        B.check(status)
     return out
 
 
@@ -233,29 +263,34 @@ def distill(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logprob: to
     """ws_distill on a student's logits [rows, cols] and a teacher's top entries [rows, k] (logprobs()' top_idx and
     top_logprob; int32 or int64 indices).  tail: the teacher's remaining mass is one more class, else its entries
     are renormalised.  weight: float32 [rows].  out: a Distill to write into (its grad may be the logits)."""
-    rows, cols, stride, dtype = _matrix(logits, "logits")
+    rows, cols, stride, dtype, device = _matrix(logits, "logits")
     if teacher_idx.dim() != logits.dim():
         raise ValueError("teacher_idx must have as many dimensions as the logits")
     k = teacher_idx.shape[-1]
-    device = logits.get_device()
-    other = _other_stream(stream, device)
+    if device != _current_device():
+        raise _elsewhere(device, "logits")
+    other = None if stream is None else _other_stream(stream, device)
     if out is None:
-        out = _results(other, lambda: Distill(
-            torch.empty(rows, dtype=torch.float32, device=logits.device),
-            torch.empty(logits.shape, dtype=logits.dtype, device=logits.device) if grad else None))
+        out = _results(other, _new_distill, rows, logits, grad)
     gptr, gstride = None, cols
     if out.grad is not None:
-        g_rows, g_cols, gstride, g_dtype = _matrix(out.grad, "out.grad")
+        g_rows, g_cols, gstride, g_dtype, where = _matrix(out.grad, "out.grad")
+        if where != device:
+            raise ValueError(f"out.grad is on another device than the call's cuda:{device}")
         if (g_rows, g_cols, g_dtype) != (rows, cols, dtype):
             raise ValueError("out.grad has another shape or type than the logits")
         gptr = out.grad.data_ptr()
     entries = (rows, k) if logits.dim() == 2 else (k,)
-    ids = _operand(teacher_idx, "teacher_idx", entries, _INDEX_TYPES)
+    ids = _operand(teacher_idx, "teacher_idx", entries, _INDEX_TYPES, device)
     desc = B.ws_distill_desc(rows, cols, stride, gstride, dtype, _INDEX_TYPES[teacher_idx.dtype], k,
                              B.WS_DISTILL_TAIL if tail else B.WS_DISTILL_RENORM, temperature)
-    B.check(B.ws_distill(desc, logits.data_ptr(), ids, _operand(teacher_logprob, "teacher_logprob", entries, _F32),
-                         _operand(weight, "weight", (rows,), _F32), _operand(out.loss, "out.loss", (rows,), _F32), gptr,
-                         _keep(other, device, logits, teacher_idx, teacher_logprob, weight, *out)))
+    status = B.ws_distill(desc, logits.data_ptr(), ids,
+                          _operand(teacher_logprob, "teacher_logprob", entries, _F32, device),
+                          _operand(weight, "weight", (rows,), _F32, device),
+                          _operand(out.loss, "out.loss", (rows,), _F32, device), gptr, _current_stream(device) if other is None else
+                          _held(other, logits, teacher_idx, teacher_logprob, weight, *out))
+    if status:
+        B.check(status)
     return out
 
 
@@ -278,16 +313,19 @@ def detect(head: torch.Tensor, desc: B.ws_detect_desc, workspace: torch.Tensor |
     if head.dtype != torch.float32 or not head.is_cuda or not head.is_contiguous() or head.dim() != 3:
         raise TypeError("head must be a contiguous float32 CUDA tensor [batch, channels, anchors]")
     batch = head.shape[0]
+    device = head.get_device()
+    if device != _current_device():
+        raise _elsewhere(device, "head")
+    other = None if stream is None else _other_stream(stream, device)
     if workspace is None:
         workspace = detect_workspace(desc, batch, head.device, stream)
-    device = head.get_device()
-    other = _other_stream(stream, device)
     if out is None:
-        out = _results(other, lambda: torch.empty((batch, desc.max_det, 8), dtype=torch.int32, device=head.device))
+        out = _results(other, _empty, (batch, desc.max_det, 8), torch.int32, head.device)
     if out_count is None:
-        out_count = _results(other, lambda: torch.empty(batch, dtype=torch.int32, device=head.device))
+        out_count = _results(other, _empty, (batch,), torch.int32, head.device)
     B.check(B.ws_detect(desc, head.data_ptr(), batch, out.data_ptr(), out_count.data_ptr(), workspace.data_ptr(),
-                        workspace.numel(), _keep(other, device, head, out, out_count, workspace)))
+                        workspace.numel(),
+                        _current_stream(device) if other is None else _held(other, head, out, out_count, workspace)))
     return out, out_count
 
 
