@@ -352,7 +352,8 @@ ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const vo
  *   grad_entropy:  device, float32 [rows], or NULL for 0.
  *   grad_logits:   device, [rows][grad_stride] of the logits' type, each
  *                  value rounded once from float32; may be the logits
- *                  themselves (same pointer, grad_stride = row_stride).
+ *                  themselves (same pointer, grad_stride = row_stride), else
+ *                  its rows share no element with theirs (refused).
  * A row in which nothing is left has gradient 0; a row with a +inf logit, or
  * whose token is >= cols (error bit 0x8), has NaN.  desc->k is not used.
  * Errors: as ws_logprobs; grad_stride < cols. */
@@ -396,7 +397,8 @@ ws_status ws_distill_validate(const ws_distill_desc* desc);
  *   grad_logits:     device, [rows][grad_stride] of the logits' type: weight *
  *                    dL/dlogits, each value rounded once from float32; NULL
  *                    for the loss alone.  May be the logits themselves (same
- *                    pointer, grad_stride = row_stride).
+ *                    pointer, grad_stride = row_stride), else its rows share
+ *                    no element with theirs (refused).
  * With q the teacher's probabilities of its entries (renormalised to sum to 1
  * or as given), p the student's over all columns, and T the temperature:
  *   RENORM: L = sum q_i (ln q_i - ln p_i);

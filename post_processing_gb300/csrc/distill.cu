@@ -1155,9 +1155,10 @@ ws_status ws_distill(const ws_distill_desc* desc, const void* logits, const void
     WS_TRY(check_pointer(teacher_logprob, 4, "teacher_logprob"));
     if (weight) WS_TRY(check_pointer(weight, 4, "weight"));
     WS_TRY(check_pointer(loss, 4, "loss"));
-    if (grad_logits) WS_TRY(check_pointer(grad_logits, size, "grad_logits"));
-    if (logits == grad_logits && desc->rows > 1 && desc->grad_stride != desc->row_stride)
-        return fail(WS_ERR_INVALID_ARGUMENT, "grad_logits in place with another stride");
+    if (grad_logits) {
+        WS_TRY(check_pointer(grad_logits, size, "grad_logits"));
+        WS_TRY(check_gradient(logits, desc->row_stride, grad_logits, desc->grad_stride, desc->rows, desc->cols, size));
+    }
 
     int dev;
     const DeviceInfo* info;

@@ -1475,8 +1475,7 @@ ws_status ws_logprobs_backward(const ws_logprobs_desc* desc, const void* logits,
     if (grad_stride < desc->cols)
         return fail(WS_ERR_INVALID_ARGUMENT, "grad_stride %lld < cols %lld", (long long)grad_stride, (long long)desc->cols);
     if (desc->rows > (1LL << 40) / grad_stride) return fail(WS_ERR_INVALID_ARGUMENT, "rows * grad_stride too large");
-    if (logits == grad_logits && desc->rows > 1 && grad_stride != desc->row_stride)
-        return fail(WS_ERR_INVALID_ARGUMENT, "grad_logits in place with another stride");
+    WS_TRY(check_gradient(logits, desc->row_stride, grad_logits, grad_stride, desc->rows, desc->cols, size));
     if (grad_logprob) {
         WS_TRY(check_pointer(grad_logprob, 4, "grad_logprob"));
         WS_TRY(check_pointer(tokens, desc->index_type == WS_INDEX_I64 ? 8 : 4, "tokens"));

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ws_host.h"
 #include "ws_internal.cuh"
 #include "ws_ptx.cuh"
 
@@ -410,6 +411,20 @@ inline ws_status check_pointer(const void* p, size_t size, const char* name) {
     if (!p) return fail(WS_ERR_INVALID_ARGUMENT, "%s is NULL", name);
     if (reinterpret_cast<uintptr_t>(p) % size != 0)
         return fail(WS_ERR_INVALID_ARGUMENT, "%s is not aligned to its %zu-byte elements", name, size);
+    return WS_OK;
+}
+
+// A gradient goes to the logits' own rows or to rows that share no element
+// with them: of others, some would be written before they are read.
+inline ws_status check_gradient(const void* logits, int64_t row_stride, const void* grad, int64_t grad_stride, int64_t rows,
+                                int64_t cols, size_t size) {
+    if (logits == grad) {
+        if (rows > 1 && grad_stride != row_stride)
+            return fail(WS_ERR_INVALID_ARGUMENT, "grad_logits in place with another stride");
+        return WS_OK;
+    }
+    if (rows_overlap(logits, row_stride, grad, grad_stride, rows, cols, size))
+        return fail(WS_ERR_INVALID_ARGUMENT, "grad_logits overlaps the logits");
     return WS_OK;
 }
 
