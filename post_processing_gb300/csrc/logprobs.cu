@@ -1241,9 +1241,7 @@ constexpr int kRingStages[kRings] = {3, 5, kMaxStages};
 // Clusters of 2^i blocks that the device holds at once with rings of that many
 // chunks (0: it cannot place one; 16 blocks are a size that it need not
 // support).
-struct Resident {
-    int clusters[kRings][kClusterSizes];
-};
+using Resident = AskedOnce<kRings, kClusterSizes>;
 
 ForwardPlan plan_forward(long long rows, long long nvec, int sm_count, const Resident& resident) {
     ForwardPlan f{};
@@ -1274,7 +1272,7 @@ ForwardPlan plan_forward(long long rows, long long nvec, int sm_count, const Res
     // 10.4 (256).
     f.kind = ForwardPlan::kCluster;
     int cluster = 1;
-    while (cluster < kMaxCluster && rows <= resident.clusters[0][f.cluster_log2 + 1] &&
+    while (cluster < kMaxCluster && rows <= resident.of[0][f.cluster_log2 + 1] &&
            nvec / (2 * cluster) >= (rows * cluster <= sm_count ? 1 : 8) * kThreads) {
         cluster *= 2;
         ++f.cluster_log2;
@@ -1290,7 +1288,7 @@ ForwardPlan plan_forward(long long rows, long long nvec, int sm_count, const Res
     // 9.8, with three 30.7 and 13.0; [8,1000000] f32 takes 18.4 us with three,
     // and 30.7 with eight, of which not all find room.
     int ring = 0;
-    while (ring + 1 < kRings && rows <= resident.clusters[ring + 1][f.cluster_log2]) ++ring;
+    while (ring + 1 < kRings && rows <= resident.of[ring + 1][f.cluster_log2]) ++ring;
     f.stages = (int)std::min<long long>(chunks, kRingStages[ring]);
     f.resident = f.stages >= chunks;
     f.group = (int)((chunks + kMaxima - 1) / kMaxima);
@@ -1314,35 +1312,34 @@ cudaError_t set_attributes(int dev) {
     return e;
 }
 
-// Fills in what the device holds at once; asked once per device.
-const Resident& resident_clusters(int dev) {
+// What the device holds at once; asked once per device.
+Resident resident_clusters(int dev) {
     static std::mutex mu;
     static Resident known[64];
-    static bool asked[64];
     std::lock_guard<std::mutex> lock(mu);
     Resident& of = known[dev];
-    if (asked[dev]) return of;
-    const auto kernel = logprobs_kernel<ElemF16, true, 4>;
-    bool ok = set_attributes<ElemF16, true, 4>(dev) == cudaSuccess;
-    for (int ring = 0; ring < kRings; ++ring)
-        for (int i = 0; i < kClusterSizes; ++i) {
+    of.ask(
+        [&] {
+            const bool ok = set_attributes<ElemF16, true, 4>(dev) == cudaSuccess;
+            if (!ok) (void)cudaGetLastError();
+            return ok;
+        },
+        [&](int ring, int size, int* n) {
             cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(1u << i);
+            cfg.gridDim = dim3(1u << size);
             cfg.blockDim = dim3(kThreads + 32);
             cfg.dynamicSmemBytes = dynamic_memory(kRingStages[ring], 4, true);
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.x = 1u << size;
             attr[0].val.clusterDim.y = 1;
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            int n = 0;
-            ok = ok && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess;
-            of.clusters[ring][i] = ok ? n : 0;
-        }
-    (void)cudaGetLastError();
-    asked[dev] = true;
+            const bool ok = cudaOccupancyMaxActiveClusters(n, logprobs_kernel<ElemF16, true, 4>, &cfg) == cudaSuccess;
+            if (!ok) (void)cudaGetLastError();
+            return ok;
+        });
     return of;
 }
 

@@ -27,4 +27,26 @@ inline bool rows_overlap(const void* a, int64_t sa, const void* b, int64_t sb, i
     return false;
 }
 
+// Answers of queries that are asked once: at most kA x kB whole numbers, 0 for
+// a query that fails (a cluster size that a device need not support, say)
+// whatever became of the others.  Where what the queries need cannot be
+// prepared, nothing is kept, and the next call asks again.
+template <int kA, int kB>
+struct AskedOnce {
+    int of[kA][kB] = {};
+    bool asked = false;
+
+    // prepare() -> bool; query(a, b, &answer) -> bool.
+    template <class Prepare, class Query>
+    void ask(Prepare prepare, Query query) {
+        if (asked || !prepare()) return;
+        for (int a = 0; a < kA; ++a)
+            for (int b = 0; b < kB; ++b) {
+                int n = 0;
+                of[a][b] = query(a, b, &n) ? n : 0;
+            }
+        asked = true;
+    }
+};
+
 }  // namespace ws

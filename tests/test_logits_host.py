@@ -73,3 +73,34 @@ def test_gradients_that_overlap_the_logits_are_refused(B):
         # one row: strides do not matter
         desc = B.ws_distill_desc(1, 100, 1000, 700, dtype, B.WS_INDEX_I32, 5, B.WS_DISTILL_TAIL, 1.0)
         assert B.ws_distill(desc, x, 64, 64, 64, 64, x + 7 * size, 0) == B.WS_ERR_INVALID_ARGUMENT
+
+
+def test_each_query_counts_for_itself(tmp_path):
+    """A query that fails leaves the others' answers; answers are kept once the queries could be prepared, and not before."""
+    exe = compiled(tmp_path, r'''
+int main() {
+    ws::AskedOnce<3, 5> t;
+    int prepared = 0, queries = 0;
+    auto show = [&] {
+        for (auto& row : t.of) for (int n : row) printf("%d ", n);
+        printf("%d %d %d\n", (int)t.asked, prepared, queries);
+    };
+    auto query = [&](int a, int b, int* n) {
+        ++queries;
+        *n = 77;                          // what a failed query leaves there does not count
+        if (b == 4 || (a == 0 && b == 1)) return false;
+        *n = 10 * a + b + 1;
+        return true;
+    };
+    t.ask([&] { ++prepared; return false; }, query);
+    show();
+    t.ask([&] { ++prepared; return true; }, query);
+    show();
+    t.ask([&] { ++prepared; return true; }, query);
+    show();
+}''')
+    out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split("\n")
+    kept = "1 0 3 4 0 11 12 13 14 0 21 22 23 24 0"
+    assert out[0].strip() == "0 " * 15 + "0 1 0"
+    assert out[1].strip() == kept + " 1 2 15"
+    assert out[2].strip() == kept + " 1 2 15"
