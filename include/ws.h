@@ -301,7 +301,10 @@ ws_status ws_topk_noalloc(const float* x, int64_t rows, int64_t cols, int32_t k,
  * A row may be read in 16-byte blocks that hold bytes of it (up to 15 bytes
  * before and after the row, never used).  Each call is one kernel launch on
  * `stream`, a programmatic dependent of the kernel before it, needs no
- * workspace, allocates nothing and may be captured into a CUDA Graph. */
+ * workspace, allocates nothing and may be captured into a CUDA Graph.  After
+ * error bit 0x1 (ws_device_error; a copy did not come in time) the rows
+ * concerned are not valid: ws_logprobs writes NaN (lse +inf) and -1 for top
+ * entries that it has not read, ws_distill may leave rows unwritten. */
 #define WS_INDEX_I32 0         /* tokens and teacher indices are int32                  */
 #define WS_INDEX_I64 1         /* ... int64                                            */
 
@@ -340,6 +343,18 @@ ws_status ws_logprobs_validate(const ws_logprobs_desc* desc);
 ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const void* tokens, float* logprob,
                       float* entropy, float* lse, float* stats, float* top_logprob, int32_t* top_idx,
                       cudaStream_t stream);
+
+/* Failure-path diagnostic: ws_logprobs on rows that a cluster of blocks reads
+ * (few and long ones), where one warp of the last block of odd rows, and of
+ * every block of even rows, issues no copy, so that bounded waits that nothing
+ * completes run out after limit_us (1 .. 1e6); see ws_selftest_wait_timeout.
+ * The rows' results are those of copies that did not come in time: the error
+ * word's bit 0x1, NaN (lse +inf), and top_idx the first of what was read, -1
+ * where nothing was.  WS_ERR_UNSUPPORTED for rows that are read otherwise. */
+ws_status ws_logprobs_selftest_wait_timeout(const ws_logprobs_desc* desc, const void* logits, const void* tokens,
+                                            float* logprob, float* entropy, float* lse, float* stats,
+                                            float* top_logprob, int32_t* top_idx, uint32_t limit_us,
+                                            cudaStream_t stream);
 
 /* Gradient of ws_logprobs with respect to the logits, from the gradients of
  * its log probabilities and entropies:

@@ -129,6 +129,7 @@ SIGNATURES = {
     "ws_topk_noalloc": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp]),
     "ws_logprobs_validate": (_i32, [ctypes.POINTER(ws_logprobs_desc)]),
     "ws_logprobs": (_i32, [ctypes.POINTER(ws_logprobs_desc)] + [_vp] * 9),
+    "ws_logprobs_selftest_wait_timeout": (_i32, [ctypes.POINTER(ws_logprobs_desc)] + [_vp] * 8 + [_u32, _vp]),
     "ws_logprobs_backward": (_i32, [ctypes.POINTER(ws_logprobs_desc)] + [_vp] * 7 + [_i64, _vp]),
     "ws_distill_validate": (_i32, [ctypes.POINTER(ws_distill_desc)]),
     "ws_distill": (_i32, [ctypes.POINTER(ws_distill_desc)] + [_vp] * 7),
@@ -280,6 +281,13 @@ def ws_logprobs(desc: ws_logprobs_desc, logits: int, tokens: int | None, logprob
                 stream: int = 0) -> int:
     return lib.ws_logprobs(ctypes.byref(desc), logits, tokens, logprob, entropy, lse, stats, top_logprob, top_idx,
                            stream)
+
+
+def ws_logprobs_selftest_wait_timeout(desc: ws_logprobs_desc, logits: int, tokens: int | None, logprob: int | None,
+                                      entropy: int | None, lse: int | None, stats: int | None, top_logprob: int | None,
+                                      top_idx: int | None, limit_us: int, stream: int = 0) -> int:
+    return lib.ws_logprobs_selftest_wait_timeout(ctypes.byref(desc), logits, tokens, logprob, entropy, lse, stats,
+                                                 top_logprob, top_idx, limit_us, stream)
 
 
 def ws_logprobs_backward(desc: ws_logprobs_desc, logits: int, tokens: int | None, stats: int, entropy: int | None,

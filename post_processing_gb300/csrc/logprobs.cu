@@ -83,6 +83,8 @@ struct LogprobsParams {
     float* top_logprob;
     int* top_idx;
     uint32_t* err;
+    unsigned long long wait_ns;   // the limit of a wait for a copy
+    int withhold;                 // a self-test: the last warp of odd rows' last block, and of even rows' every block, fetches nothing
 };
 
 // What a row's results are made of.
@@ -128,6 +130,12 @@ __device__ __forceinline__ void write_top(const LogprobsParams& p, long long row
                                           unsigned long long key) {
     p.top_logprob[row * p.k + at] = entry_logprob(r, order_value((uint32_t)(key >> 32)), p.temperature);
     p.top_idx[row * p.k + at] = (int)key_index(key);
+}
+
+// Entry `at` of a row whose copies did not come in time, where no key is left for it.
+__device__ __forceinline__ void write_lost(const LogprobsParams& p, long long row, int at) {
+    p.top_logprob[row * p.k + at] = NAN;
+    p.top_idx[row * p.k + at] = -1;
 }
 
 // The largest entry of a vector (NaN gives way).
@@ -812,6 +820,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) logprobs_kernel(const __grid
         uint32_t pending = 0;   // bit i: a copy into stage i has not been waited for
         constexpr int kStride = kWarps * kChunk;   // from one chunk of the warp to its next
         int next = start + warp * kChunk;          // the next chunk to fetch
+        if (p.withhold && warp == kWarps - 1 && (rank == C - 1 || row % 2 == 0)) next = v1;
         auto fetch = [&](int st) {                 // into stage st, if anything is left
             if (next >= v1) return;
             pending |= 1u << st;
@@ -837,7 +846,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) logprobs_kernel(const __grid
         int g_left = p.group;
         for (int vb = start + warp * kChunk; vb < v1; vb += kStride) {
             const int st = stage;
-            if (!__all_sync(kFull, mbar_wait_bounded(&s.bar[warp][st], (phase >> st) & 1u, kWaitLimitNs))) {
+            if (!__all_sync(kFull, mbar_wait_bounded(&s.bar[warp][st], (phase >> st) & 1u, p.wait_ns))) {
                 ok = false;
                 break;
             }
@@ -1076,6 +1085,11 @@ __global__ void __launch_bounds__(kThreads + 32, 3) logprobs_kernel(const __grid
         const SoftSums total = lane_sums(s.cpart, C, p.c);
         r = row_result(total);
         if (rank == 0 && lane == 0) write_row(p, row, total, r, s.token, s.x_tok);
+        if (kTop && rank == 0 && r.bad) {   // blocks that lost their runs have no keys
+            int keys = C == 1 && !s.late ? p.k : 0;
+            for (int i = 0; C > 1 && i < C; ++i) keys += __popc(__ballot_sync(kFull, lists[i][lane] != 0ull));
+            if (lane >= keys && lane < p.k) write_lost(p, row, lane);
+        }
     }
     if constexpr (kTop) {
         if (C > 1) {
@@ -1381,20 +1395,10 @@ cudaError_t launch_forward(const LogprobsParams& p, const ForwardPlan& f, int de
     }
 }
 
-}  // namespace
-}  // namespace ws
-
-extern "C" {
-
-ws_status ws_logprobs_validate(const ws_logprobs_desc* desc) {
-    ws::clear_error();
-    return ws::validate_desc(desc);
-}
-
-ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const void* tokens, float* logprob,
-                      float* entropy, float* lse, float* stats, float* top_logprob, int32_t* top_idx,
-                      cudaStream_t stream) {
-    using namespace ws;
+// The forward call; selftest_us: the limit of ws_logprobs_selftest_wait_timeout, else 0.
+ws_status enqueue_logprobs(const ws_logprobs_desc* desc, const void* logits, const void* tokens, float* logprob,
+                           float* entropy, float* lse, float* stats, float* top_logprob, int32_t* top_idx,
+                           uint32_t selftest_us, cudaStream_t stream) {
     clear_error();
     WS_TRY(validate_desc(desc));
     const size_t size = elem_size(desc->dtype);
@@ -1420,6 +1424,8 @@ ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const vo
     const bool aligned = (uintptr_t)logits % 16 == 0 && (desc->rows == 1 || desc->row_stride % per == 0);
     const long long nvec = aligned ? (desc->cols + per - 1) / per : max_vectors(desc->cols, per);
     const ForwardPlan f = plan_forward(desc->rows, nvec, info->sm_count, resident_clusters(dev));
+    if (selftest_us && f.kind != ForwardPlan::kCluster)
+        return fail(WS_ERR_UNSUPPORTED, "these rows are read without bounded waits");
     LogprobsParams p{};
     p.x = logits;
     p.stride = desc->row_stride;
@@ -1442,6 +1448,8 @@ ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const vo
     p.top_logprob = top_logprob;
     p.top_idx = top_idx;
     p.err = device_error_word();
+    p.wait_ns = selftest_us ? 1000ull * selftest_us : kWaitLimitNs;
+    p.withhold = selftest_us != 0;
     if (desc->rows > 2147483647LL) return fail(WS_ERR_UNSUPPORTED, "too many rows");
     cudaError_t e;
     const bool top = desc->k > 0;
@@ -1456,6 +1464,32 @@ ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const vo
                 : launch_forward<ElemBF16, false>(p, f, dev, info->sm_count, stream);
     if (e != cudaSuccess) return cuda_fail(e, "log-probability launch");
     return WS_OK;
+}
+
+}  // namespace
+}  // namespace ws
+
+extern "C" {
+
+ws_status ws_logprobs_validate(const ws_logprobs_desc* desc) {
+    ws::clear_error();
+    return ws::validate_desc(desc);
+}
+
+ws_status ws_logprobs(const ws_logprobs_desc* desc, const void* logits, const void* tokens, float* logprob,
+                      float* entropy, float* lse, float* stats, float* top_logprob, int32_t* top_idx,
+                      cudaStream_t stream) {
+    return ws::enqueue_logprobs(desc, logits, tokens, logprob, entropy, lse, stats, top_logprob, top_idx, 0, stream);
+}
+
+ws_status ws_logprobs_selftest_wait_timeout(const ws_logprobs_desc* desc, const void* logits, const void* tokens,
+                                            float* logprob, float* entropy, float* lse, float* stats,
+                                            float* top_logprob, int32_t* top_idx, uint32_t limit_us,
+                                            cudaStream_t stream) {
+    ws::clear_error();
+    if (limit_us < 1 || limit_us > 1000000)
+        return ws::fail(WS_ERR_INVALID_ARGUMENT, "limit_us %u outside 1..1000000", limit_us);
+    return ws::enqueue_logprobs(desc, logits, tokens, logprob, entropy, lse, stats, top_logprob, top_idx, limit_us, stream);
 }
 
 ws_status ws_logprobs_backward(const ws_logprobs_desc* desc, const void* logits, const void* tokens,
