@@ -192,6 +192,12 @@ def _new_logprobs(rows: int, k: int, with_tokens: bool, device) -> Logprobs:
                     torch.empty((rows, k), dtype=torch.int32, device=device) if k else None)
 
 
+def _spent(logits: torch.Tensor) -> None:
+    """Logits that were overwritten by their gradient: autograd is told, so that a graph that saved them says so when it
+    is run backward, in place of using what is there now."""
+    torch.autograd.graph.increment_version(logits)
+
+
 def _new_distill(rows: int, logits: torch.Tensor, grad: bool) -> Distill:
     return Distill(_empty((rows,), torch.float32, logits.device),
                    _empty(logits.shape, logits.dtype, logits.device) if grad else None)
@@ -201,7 +207,10 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
              out: Logprobs | None = None, stream=None) -> Logprobs:
     """ws_logprobs on a CUDA tensor [rows, cols] (or [cols]) of float32, float16 or bfloat16, whose rows may be
     padded.  tokens: int32 or int64 [rows], negative where a row has none.  out: an earlier result of the same
-    call to write into."""
+    call to write into.
+
+    Results carry no autograd history, whether or not the logits require a gradient: a loss on them is
+    differentiated by logprobs_backward(), whose gradient goes on by logits.backward(gradient)."""
     rows, cols, stride, dtype, device = _matrix(logits, "logits")
     if device != _current_device():
         raise _elsewhere(device, "logits")
@@ -230,7 +239,8 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats: 
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """ws_logprobs_backward: the gradient of the logits from those of logprobs()' log probabilities and entropies
     (either may be None); stats and entropy as logprobs() gave them.  out: a tensor of the logits' shape and type
-    whose rows may be padded, the logits themselves included."""
+    whose rows may be padded, the logits themselves included (they are spent then, and autograd's version of them
+    counts up); other rows that overlap the logits' are refused."""
     rows, cols, stride, dtype, device = _matrix(logits, "logits")
     if device != _current_device():
         raise _elsewhere(device, "logits")
@@ -245,15 +255,18 @@ def logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, stats: 
     per_row = (rows,)
     desc = B.ws_logprobs_desc(rows, cols, stride, dtype, _INDEX_TYPES.get(tokens.dtype, 0) if tokens is not None else 0,
                               0, temperature)
-    status = B.ws_logprobs_backward(desc, logits.data_ptr(), _operand(tokens, "tokens", per_row, _INDEX_TYPES, device),
+    at, to = logits.data_ptr(), out.data_ptr()
+    status = B.ws_logprobs_backward(desc, at, _operand(tokens, "tokens", per_row, _INDEX_TYPES, device),
                                     _operand(stats, "stats", (rows, 2), _F32, device),
                                     _operand(entropy, "entropy", per_row, _F32, device),
                                     _operand(grad_logprob, "grad_logprob", per_row, _F32, device),
-                                    _operand(grad_entropy, "grad_entropy", per_row, _F32, device), out.data_ptr(),
-                                    out_stride, _current_stream(device) if other is None else _held(
+                                    _operand(grad_entropy, "grad_entropy", per_row, _F32, device), to, out_stride,
+                                    _current_stream(device) if other is None else _held(
                                         other, logits, tokens, stats, entropy, grad_logprob, grad_entropy, out))
     if status:
         B.check(status)
+    if to == at:
+        _spent(out)
     return out
 
 
@@ -262,7 +275,9 @@ def distill(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logprob: to
             out: Distill | None = None, stream=None) -> Distill:
     """ws_distill on a student's logits [rows, cols] and a teacher's top entries [rows, k] (logprobs()' top_idx and
     top_logprob; int32 or int64 indices).  tail: the teacher's remaining mass is one more class, else its entries
-    are renormalised.  weight: float32 [rows].  out: a Distill to write into (its grad may be the logits)."""
+    are renormalised.  weight: float32 [rows].  out: a Distill to write into (its grad may be the logits,
+    as for logprobs_backward()).  The loss carries no autograd history; the gradient goes on by
+    logits.backward(grad)."""
     rows, cols, stride, dtype, device = _matrix(logits, "logits")
     if teacher_idx.dim() != logits.dim():
         raise ValueError("teacher_idx must have as many dimensions as the logits")
@@ -284,13 +299,16 @@ def distill(logits: torch.Tensor, teacher_idx: torch.Tensor, teacher_logprob: to
     ids = _operand(teacher_idx, "teacher_idx", entries, _INDEX_TYPES, device)
     desc = B.ws_distill_desc(rows, cols, stride, gstride, dtype, _INDEX_TYPES[teacher_idx.dtype], k,
                              B.WS_DISTILL_TAIL if tail else B.WS_DISTILL_RENORM, temperature)
-    status = B.ws_distill(desc, logits.data_ptr(), ids,
+    at = logits.data_ptr()
+    status = B.ws_distill(desc, at, ids,
                           _operand(teacher_logprob, "teacher_logprob", entries, _F32, device),
                           _operand(weight, "weight", (rows,), _F32, device),
                           _operand(out.loss, "out.loss", (rows,), _F32, device), gptr, _current_stream(device) if other is None else
                           _held(other, logits, teacher_idx, teacher_logprob, weight, *out))
     if status:
         B.check(status)
+    if gptr == at:
+        _spent(out.grad)
     return out
 
 

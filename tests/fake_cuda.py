@@ -77,6 +77,7 @@ class Cuda:
         monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current_device)
         monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device=None: Stream(raw))
+        monkeypatch.setattr(torch.autograd.graph, "increment_version", lambda t: None)
         monkeypatch.setattr(api, "_current_stream", lambda device: self.streams[-1].cuda_stream)
         if hasattr(api, "_current_device"):
             monkeypatch.setattr(api, "_current_device", lambda: self.current_device)
