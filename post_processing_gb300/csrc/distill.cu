@@ -222,7 +222,7 @@ __device__ __forceinline__ float row_loss(const DistillParams& p, const RowExcha
     for (int k = lane; k < p.k; k += 32) {
         const float x = r.x[k], q = q_of[k];
         // the student's log probability; -inf where it is masked
-        const float lp = x > -INFINITY ? (x - t.m) * p.inv_t - ln_s : -INFINITY;
+        const float lp = x > -INFINITY ? half_gap(x, t.m) * (2.f * p.inv_t) - ln_s : -INFINITY;
         if (q > 0.f) term += q * (r.lq[k] - lp);
         more += exp2_fast(below(x, t.m) * p.c) * per_total - q;
     }
@@ -239,7 +239,7 @@ __device__ __forceinline__ float row_loss(const DistillParams& p, const RowExcha
             const float rel = more / (t.off * t.per_off * per_total);
             loss += teacher.rest * (rel > -0.5f && rel < 1.f
                                         ? log1pf(rel)
-                                        : logf(teacher.rest) - ((t.m_off - t.m) * p.inv_t + (logf(t.off) - ln_s)));
+                                        : logf(teacher.rest) - (half_gap(t.m_off, t.m) * (2.f * p.inv_t) + (logf(t.off) - ln_s)));
         } else {
             loss = INFINITY;
         }

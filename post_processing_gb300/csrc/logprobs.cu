@@ -104,7 +104,7 @@ __device__ __forceinline__ RowResult row_result(const SoftSums& a) {
 __device__ __forceinline__ float entry_logprob(const RowResult& r, float x, float temperature) {
     if (r.bad) return NAN;
     if (!(x > -INFINITY)) return -INFINITY;
-    return (x - r.m) / temperature - r.ln_s;
+    return half_gap(x, r.m) / (0.5f * temperature) - r.ln_s;
 }
 
 // One thread writes what a row has one of.

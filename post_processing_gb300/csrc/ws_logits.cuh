@@ -192,6 +192,11 @@ struct SoftSums {
 
 __device__ __forceinline__ float below(float x, float m) { return fmaxf(x - m, kLowest); }
 
+// Half of x - m for finite x and m: the difference itself passes float32's
+// range for entries near both ends of it, where its quotient by a temperature
+// need not.  (Halves are exact but for subnormal entries.)
+__device__ __forceinline__ float half_gap(float x, float m) { return fmaf(0.5f, x, -0.5f * m); }
+
 // The sums restated relative to m >= a.m (a.m = -inf: no entry yet).  The
 // difference meets its factor first: -3e38 times 0 is 0, where s times -3e38
 // overflows.

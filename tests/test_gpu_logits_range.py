@@ -1,0 +1,45 @@
+"""Entries near both ends of float32's range: their difference passes it, the
+difference over the temperature does not."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+END = 3.0e38
+
+
+@pytest.fixture(scope="module")
+def pp():
+    import __graft_entry__
+    __graft_entry__.build()
+    import post_processing_gb300
+    return post_processing_gb300
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [8, 1000, 20001, 300001])
+@pytest.mark.parametrize("temperature", [4.0, 1000.0, 2.0 ** 20])
+def test_finite_log_probabilities_and_losses(pp, temperature, cols, dtype):
+    x = torch.full((2, cols), -np.inf, device="cuda")
+    x[:, 1], x[:, cols // 2], x[0, cols - 1] = END, -END, -END / 2
+    x = x.to(dtype)
+    v = x.double()
+    # one entry holds everything, so ln p of the others is their distance; 3 roundings of it
+    want = (v - v[:, 1:2]) / temperature
+    tok = torch.tensor([cols // 2, cols // 2], device="cuda")
+    f = pp.logprobs(x, tok, k=3, temperature=temperature)
+    close = lambda a, b: torch.allclose(a.double(), b, rtol=4 * 2.0 ** -24, atol=0.0)  # noqa: E731
+    assert want.gather(1, tok[:, None]).isfinite().all()
+    assert close(f.logprob, want.gather(1, tok[:, None]).squeeze(1))
+    assert close(f.top_logprob, want.gather(1, f.top_idx.long()))
+    assert torch.equal(f.top_idx[0].cpu(), torch.tensor([1, cols - 1, cols // 2], dtype=torch.int32))
+    # a teacher that holds 3/4 of its mass on the far entry; the tail class lies on the likely one, or on the third
+    for ids, lq in (([cols // 2], [0.75]), ([1, cols // 2], [0.5, 0.25])):
+        q = torch.tensor([lq], device="cuda").float()
+        ids = torch.tensor([ids], device="cuda")
+        got = pp.distill(x[:1], ids, q.log(), temperature=temperature, tail=True)
+        far = want[0, cols // 2].item() * lq[-1]
+        if len(lq) == 2:
+            far += 0.25 * want[0, cols - 1].item()
+        assert torch.allclose(got.loss.double().cpu(), torch.tensor([-far]).double(), rtol=1e-6)
+        assert got.grad.isfinite().all()
