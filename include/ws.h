@@ -296,8 +296,12 @@ ws_status ws_topk_noalloc(const float* x, int64_t rows, int64_t cols, int32_t k,
  * temperature and p = softmax(z).  Sums are held in float32, maxima are
  * exact, nothing depends on the order of atomics: the same inputs give the
  * same bits.  A NaN logit counts as -inf, as in the Top-K, and a -inf logit
- * is a masked entry: its probability is 0 and its gradient 0.  A row with a
+ * is a masked entry: its probability is 0 and its gradient 0, but for what the
+ * formulas add at a masked token (grad_logprob / temperature, in a row that has
+ * other entries) or teacher's column (-weight * q / temperature).  A row with a
  * +inf logit has a +inf log-sum-exp and NaN in every other floating result.
+ * A result beyond float32's range is infinite: the log-sum-exp of a finite row
+ * at a small temperature, for one (entries of 3e38 at temperatures below 1).
  * A row may be read in 16-byte blocks that hold bytes of it (up to 15 bytes
  * before and after the row, never used).  Each call is one kernel launch on
  * `stream`, a programmatic dependent of the kernel before it, needs no

@@ -405,7 +405,8 @@ inline ws_status validate_logits(int64_t rows, int64_t cols, int64_t row_stride,
         return fail(WS_ERR_INVALID_ARGUMENT, "dtype %d", dtype);
     if (index_type != WS_INDEX_I32 && index_type != WS_INDEX_I64)
         return fail(WS_ERR_INVALID_ARGUMENT, "index_type %d", index_type);
-    // negated so that NaN is refused; the limits keep entry * log2(e) / temperature far inside float32
+    // negated so that NaN is refused.  Within the limits log2(e) / temperature and its inverse are ordinary numbers;
+    // its product with a difference of entries may overflow, to -inf and thence an exponential of 0.
     if (!(temperature >= 1.0f / 1048576.0f && temperature <= 1048576.0f))
         return fail(WS_ERR_INVALID_ARGUMENT, "temperature %g outside 2^-20 .. 2^20", (double)temperature);
     return WS_OK;

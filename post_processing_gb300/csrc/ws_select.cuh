@@ -1,5 +1,7 @@
-// ws_select.cuh -- exact selection by unique 64-bit keys, shared by the Top-K
-// and the log-probability kernels.
+// ws_select.cuh -- exact selection by unique 64-bit keys: the keys' order and
+// the ranking in sorted lists, which the Top-K and the log-probability kernels
+// share, and the block's radix select, the 32-key merge and the ranking by
+// counting, which the Top-K uses.
 //
 // A key holds a value's order bits in its upper word (NaN -> -inf, -0 -> +0)
 // and the bitwise complement of its index in the lower word, so a larger key

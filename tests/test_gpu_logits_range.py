@@ -43,3 +43,31 @@ def test_finite_log_probabilities_and_losses(pp, temperature, cols, dtype):
             far += 0.25 * want[0, cols - 1].item()
         assert torch.allclose(got.loss.double().cpu(), torch.tensor([-far]).double(), rtol=1e-6)
         assert got.grad.isfinite().all()
+
+
+@pytest.mark.parametrize("cols", [100, 9000, 300001])
+def test_gradients_at_masked_tokens_and_columns(pp, cols):
+    """A masked entry has no gradient but what the formulas add at a token or a teacher's column."""
+    T = 0.5
+    x = torch.randn((2, cols), device="cuda")
+    x[0, 3], x[0, 7], x[1] = -np.inf, -np.inf, -np.inf
+    tok, g = torch.tensor([3, 3], device="cuda"), torch.tensor([2.0, 2.0], device="cuda")
+    f = pp.logprobs(x, tok, temperature=T)
+    grad = pp.logprobs_backward(x, tok, f.stats, f.entropy, g, g, temperature=T)
+    assert f.logprob[0] == -np.inf and grad[0, 3] == 2.0 / T and grad[0, 7] == 0.0
+    assert not grad[1].any()
+    q = torch.tensor([[0.5, 0.25]], device="cuda").repeat(2, 1)
+    w = torch.tensor([3.0, 3.0], device="cuda")
+    d = pp.distill(x, torch.tensor([[3, 5], [3, 5]], device="cuda"), q.log(), w, temperature=T, tail=True)
+    assert d.loss[0] == np.inf and d.loss[1] == 0.0
+    assert torch.allclose(d.grad[0, 3], torch.tensor(-3.0 * 0.5 / T, device="cuda"), rtol=1e-6) and d.grad[0, 7] == 0.0
+    assert not d.grad[1].any()
+
+
+def test_a_log_sum_exp_past_float32s_range(pp):
+    """Infinite by itself; what is relative to the maximum is not."""
+    x = torch.full((1, 300), END, device="cuda")
+    f = pp.logprobs(x, torch.tensor([5], device="cuda"), k=2, temperature=0.5)
+    assert f.lse.item() == np.inf and f.stats[0, 0] == x[0, 0]
+    for v in (f.logprob, f.top_logprob, -f.entropy, -f.stats[:, 1]):
+        assert torch.allclose(v, torch.full_like(v, -np.log(300.0)), rtol=1e-6)
