@@ -71,3 +71,21 @@ def test_a_log_sum_exp_past_float32s_range(pp):
     assert f.lse.item() == np.inf and f.stats[0, 0] == x[0, 0]
     for v in (f.logprob, f.top_logprob, -f.entropy, -f.stats[:, 1]):
         assert torch.allclose(v, torch.full_like(v, -np.log(300.0)), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("temperature", [2.0 ** -20, 0.0625, 17.0, 2.0 ** 20])
+def test_gradients_over_the_accepted_temperatures(pp, temperature, dtype):
+    """With logits of a fixed size, with ones that go by the temperature, and with a mask of the type's lowest value; the
+    bounds of test_gpu_logits.py."""
+    import test_gpu_logits as base
+    g = np.random.default_rng(11)
+    for cols in (100, 5003, 40003):
+        for scale in (2.0, 4.0 * temperature):
+            y = np.clip(g.normal(0.0, scale, (4, cols)), -6e4, 6e4)
+            y[3, cols // 2:] = base.LOWEST[dtype]
+            x, xd = base.placed(y, dtype)
+            tokens = np.array([cols // 3, 0, -1, cols - 1])
+            # gradients that leave float16's range by themselves are not compared: scaled to it
+            a = (g.normal(0, 1, 4) * min(temperature, 1.0)).astype(np.float32)
+            base.check_backward(pp, x, xd, dtype, tokens, a, (a * 0.1).astype(np.float32), temperature)
