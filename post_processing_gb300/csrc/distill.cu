@@ -435,8 +435,8 @@ __device__ __forceinline__ void store_run(const DistillParams& p, typename E::St
 
 // A warp a row of at most 32 * kH vectors.  The row lies in shared memory
 // while the teacher's entries are taken out of it; after that nothing but
-// shuffles.  Bound by its chain with few rows (3.6 us for [8,1000] f32, 5
-// entries), by instructions with many: [20000,1000] f32 43.7 us, 3.7 TB/s.
+// shuffles.  Bound by its chain with few rows (3.7 us for [8,1000] f32, 5
+// entries), by instructions with many: [20000,1000] f32 37.9 us, 4.2 TB/s.
 template <class E, int kH>
 __global__ void __launch_bounds__(128, 4) distill_short_kernel(const __grid_constant__ DistillParams p) {
     using S = typename E::Storage;
@@ -582,7 +582,7 @@ struct LiveRows {
 // another; registers (96 a thread, the exponentials) and shared memory bound
 // how many those are.  Bound by that latency: [2048,131072] bf16 with 32
 // entries and the tail class takes 192 us, 5.6 TB/s of logits and gradients
-// (0.83 of a copy's), f32 392 us; [512,32000] f16 21 us, where a cluster has
+// (0.83 of a copy's), f32 410 us; [512,32000] f16 21 us, where a cluster has
 // 3.4 rows.
 //
 // The next kernel is not launched early (griddepcontrol.launch_dependents):
